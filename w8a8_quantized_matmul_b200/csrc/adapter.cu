@@ -65,7 +65,6 @@ constexpr int kMaxSmallTokens = 1024;
 constexpr int small_tokens(int R, int n) {
   return R <= 16 ? (n < 32 ? 768 : kMaxSmallTokens) : R <= 32 ? (n < 16 ? 384 : 512) : R <= 64 ? 192 : 16;
 }
-constexpr int kStatusTimeout = -5;   // == I8MM_ERR_TIMEOUT
 
 struct AdapterArgs {
   const __half* X;       // [M][K]
@@ -753,23 +752,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AdapterArgs p) {
     if (r < rounds) put(r, held[r]);
   for (int r = kHeld; r < rounds; ++r) put(r, fetch(r * kPlanThreads + tid));
   griddep_launch_dependents();
-}
-
-// Waits that give up are recorded, and the CTA does no more work after one.
-__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int32_t* stop,
-                                                int32_t* status) {
-  if (*stop) return false;
-  if (mbar_wait(bar, parity)) return true;
-  atomicCAS(status, 0, kStatusTimeout);
-  *stop = 1;
-  return false;
-}
-
-// After a wait that gave up, before the CTA ends: copies that are still in flight
-// towards its shared memory get 2 ms.
-__device__ __forceinline__ void let_copies_land() {
-  const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
 }
 
 // Shrink: a team of `split` CTAs of a cluster takes a tile of 128 tokens, each CTA a part of

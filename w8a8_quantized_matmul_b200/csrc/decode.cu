@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(64 + 32 * kMaxXWarps, 1)
   }
 
   if (!ok && lane == 0 && a.status) atomicExch(a.status, kStatusTimeout);
+  if (!ok) let_copies_land();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();   // the peer may still read our shared memory
+  if (*abort_flag) let_copies_land();
+  if constexpr (PAIR) cluster_sync();   // the peer may still read our shared memory, or copy on our barriers
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)

@@ -87,6 +87,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// A wait of a CTA whose roles share `stop` (in shared memory): the first that runs out of
+// time records it in *status (if any) and raises `stop`; every other wait for a phase
+// that is not complete, under way or still to come, then gives up too.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int32_t* stop,
+                                                int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!*stop) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (status) atomicCAS(status, 0, -5 /* I8MM_ERR_TIMEOUT */);
+      *stop = 1;
+    }
+  }
+  return false;
+}
+
+// After a wait that gave up, before the CTA ends or uses the memory for something else:
+// copies that are still in flight towards its shared memory get 2 ms. (They would land
+// in what may belong to another CTA by then.)
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------- dependent launch
 // A kernel launched with programmatic stream serialization may start before the
 // previous kernel in the stream has finished; it must execute griddep_wait()

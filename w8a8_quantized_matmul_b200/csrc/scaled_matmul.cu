@@ -40,7 +40,6 @@ constexpr int kMaxTok = 256;
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 10;
 constexpr int kThreads = 192;
-constexpr int kStatusTimeout = -5;     // == I8MM_ERR_TIMEOUT
 
 struct StreamArgs {
   const float* x_scale;   // [M]
@@ -99,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
   uint64_t* empty = full + kMaxStages;
   uint64_t* done = empty + kMaxStages;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int32_t* stop = reinterpret_cast<volatile int32_t*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = a.split;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    *stop = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     if (lane == 0) {
       for (int j = 0; j < nb; ++j) {
         const int s = j % a.stages;
-        if (!(ok = mbar_wait(&empty[s], ((j / a.stages) & 1) ^ 1))) break;
+        if (!wait_or_give_up(&empty[s], ((j / a.stages) & 1) ^ 1, stop, a.status)) break;
         uint8_t* w = sm + s * L.stage;
         const int k = (rank + j * S) * kKB;
         mbar_arrive_expect_tx(&full[s], L.stage);
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     const uint32_t idesc = make_idesc(2 /*s32*/, 1 /*signed*/, kRows, a.tok);
     for (int j = 0; j < nb && ok; ++j) {
       const int s = j % a.stages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (j / a.stages) & 1));
+      ok = __all_sync(0xffffffffu, wait_or_give_up(&full[s], (j / a.stages) & 1, stop, a.status));
       if (!ok) break;
       const uint64_t w = sw128_kmajor_desc(smem_addr(sm + s * L.stage));
       const uint64_t x = sw128_kmajor_desc(smem_addr(sm + s * L.stage + kWBytes));
@@ -155,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
         mma_i8_elect(tmem, w + 2 * kk, x + 2 * kk, idesc, (j | kk) != 0);
       mma_commit_elect(&empty[s]);
     }
-    // Always committed, so that the epilogue's wait ends after a wait that gave up here.
-    mma_commit_elect(done);
+    // `done` says that every stage has arrived and been consumed.
+    if (ok) mma_commit_elect(done);
   } else {
     const int q = warp & 3;
     const int et = tid - 64;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     named_bar_sync(1, 128);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     if (S == 1) {
-      ok = __all_sync(0xffffffffu, mbar_wait(done, 0));
+      ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, a.status));
       tc_fence_after();
       const int np = n0 + (nl & ~1);
       const float wo = __shfl_xor_sync(0xffffffffu, ws, 1);
@@ -201,8 +202,9 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
       if (warp >= 2) {
         const int q = warp & 3;
         if (c0 == 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(done, 0));
+          ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, a.status));
           tc_fence_after();
+          if (!ok) let_copies_land();               // they go where the partials will
           named_bar_sync(1, 128);
         }
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
       cluster_sync();   // read by the peers: may be overwritten, and the CTA may end
     }
   }
-  if (!ok && lane == 0 && a.status) atomicExch(a.status, kStatusTimeout);
+  if (!ok) let_copies_land();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

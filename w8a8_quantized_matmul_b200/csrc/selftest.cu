@@ -1,7 +1,8 @@
 // Self-test of the bounded device-side wait that every kernel of the library
 // uses: one CTA waits on an mbarrier phase that nothing completes. The wait
 // gives up after its time limit and the CTA records I8MM_ERR_TIMEOUT in a status
-// word, exactly as the kernels do when a wait runs out, and leaves normally.
+// word, exactly as the kernels do when a wait runs out; a second wait then gives up
+// at once, copies in flight get their time, and the CTA leaves normally.
 // No fault, trap or endless loop is involved; the GPU context stays usable.
 #include <cuda_runtime.h>
 
@@ -15,13 +16,16 @@ namespace {
 
 __global__ void wait_timeout_kernel(int32_t* status) {
   __shared__ uint64_t bar;
+  __shared__ int32_t stop;
   if (threadIdx.x == 0) {
+    stop = 0;
     mbar_init(&bar, 1);   // one arrival expected; none ever comes
     fence_mbarrier_init();
   }
   __syncthreads();
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(&bar, 0));
-  if (!ok && threadIdx.x == 0) atomicCAS(status, 0, -5 /* I8MM_ERR_TIMEOUT */);
+  for (int i = 0; i < 2; ++i) wait_or_give_up(&bar, 0, &stop, status);
+  __syncthreads();
+  if (stop) let_copies_land();
 }
 
 }  // namespace
