@@ -342,6 +342,8 @@ int int4_rotated_matmul(const void* X, const int8_t* Wq4, const float* w_absmax,
 //   x_scale = max|w| * rstd, the absmax of the row that the codes stand for
 // (rstd is common to a row, so it cancels in the codes). The statistics are of
 // the unrounded h; they are outside the contract where h^2 leaves fp32.
+// A row that meets a NaN or an infinity (in X, the residual, gamma or s_rcp) has an
+// x_scale that is not finite; its codes then mean nothing.
 //   X         in : fp16 [M][K]
 //   residual  in : fp16 [M][K], or fp32 where residual_fp32 is not 0; may be NULL
 //   gamma     in : fp16 [K]
@@ -360,6 +362,8 @@ int int8_rmsnorm_quantize_rows(const void* X, const void* residual, int residual
 // SwiGLU of each row, as INT8 codes with their scale: with g = GU[i][k] and
 // up = GU[i][I + k], in fp32, z = g / (1 + exp(-g)) * up, w = z * s_rcp (z without),
 //   Z  = fp16(z),  Zq = absmax codes of w as above,  z_scale = max|w|.
+// z is what the formula gives for a gate or an up of infinity (+inf for a gate of +inf,
+// NaN for -inf) or NaN; the row's z_scale is then not finite and its codes mean nothing.
 //   GU    in : fp16 [M][2*I], the gate's columns and then the up projection's (one
 //              product over the two weights stacked); I a multiple of 16, <= 65536
 //   s_rcp in : fp32 [I] or NULL

@@ -100,10 +100,11 @@ __device__ __forceinline__ uint4 pack_h(const Oct& a) {
   }
   return u;
 }
-// max(m, |a|, |b|)
+// max(m, |a|, |b|), NaN where one of them is: a row that holds one has to say so in its
+// scale (the instruction is the same without .NaN, which would drop it).
 __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   float r;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float absmax(const Oct& a, float m) {
@@ -181,7 +182,9 @@ __device__ __forceinline__ uint2 codes8_div(const Oct& w, float a) {
 
 // silu(g) for eight fp16 values. With a = |g| and t = e^-a <= 1, silu(g) =
 // max(g, 0) - a * t / (1 + t): nothing overflows, and nothing cancels (the second
-// term is at most half the first). t = 2^y * (1 + c), y the rounded product of -a
+// term is at most half the first). A gate of +inf, where a * t would be NaN, gives +inf:
+// a positive gate enters a as 128 at most, where t is 0 already; -inf gives NaN, as
+// g / (1 + exp(-g)) does, and so does NaN, through max(g, 0). t = 2^y * (1 + c), y the rounded product of -a
 // and log2 e and c the error of that rounding, from one more multiply-add, times ln 2.
 // With ex2.approx within 2^-22 and rcp.approx within 2^-23 the result is within 10
 // half steps of fp32 (a Newton step on the reciprocal would take one away and cost
@@ -192,8 +195,9 @@ __device__ __forceinline__ Oct silu8(const uint4& u) {
   Oct o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 af = __half22float2(habs2_bits(w[i]));
-    const float2 gf = __half22float2(__hmax2(*reinterpret_cast<const __half2*>(&w[i]), __float2half2_rn(0.0f)));
+    const __half2 g = *reinterpret_cast<const __half2*>(&w[i]);
+    const float2 af = __half22float2(__hmax2(__hneg2(g), __hmin2(g, __float2half2_rn(128.0f))));
+    const float2 gf = __half22float2(__hmax2_nan(g, __float2half2_rn(0.0f)));
     const uint64_t a = pair2(af.x, af.y);
     const uint64_t y = mul2(a, pair2(-kLog2e, -kLog2e));
     const uint64_t c = mul2(fma2(a, pair2(kLog2e, kLog2e), y), pair2(-kLn2, -kLn2));
@@ -307,12 +311,12 @@ __device__ __forceinline__ void keep_w(const RowArgs& a, const float4 (&s)[2], O
   }
 }
 
-// Sum and maximum over the T threads of a row; every thread gets them. The
+// Sum and maximum (NaN if a thread has one) over the T threads of a row; every thread gets them. The
 // barrier alone does: `red` alternates between two rows' parts.
 __device__ __forceinline__ void reduce_row(float& sq, float& top, float (*red)[2][32], uint32_t turn, int T) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  // non-negative floats order like their bit patterns
+  // non-negative floats order like their bit patterns, and the NaN of max_abs3 lies above inf
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   if (T == 32) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
