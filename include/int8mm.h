@@ -362,6 +362,8 @@ int int8_rmsnorm_quantize_rows(const void* X, const void* residual, int residual
 // SwiGLU of each row, as INT8 codes with their scale: with g = GU[i][k] and
 // up = GU[i][I + k], in fp32, z = g / (1 + exp(-g)) * up, w = z * s_rcp (z without),
 //   Z  = fp16(z),  Zq = absmax codes of w as above,  z_scale = max|w|.
+// z is within 11 half steps of fp32 of the formula's value; below g = -87.3, where
+// g / (1 + exp(-g)) is under 2^-119, it counts as 0.
 // z is what the formula gives for a gate or an up of infinity (+inf for a gate of +inf,
 // NaN for -inf) or NaN; the row's z_scale is then not finite and its codes mean nothing.
 //   GU    in : fp16 [M][2*I], the gate's columns and then the up projection's (one

@@ -180,39 +180,42 @@ __device__ __forceinline__ uint2 codes8_div(const Oct& w, float a) {
   return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
 }
 
-// silu(g) for eight fp16 values. With a = |g| and t = e^-a <= 1, silu(g) =
-// max(g, 0) - a * t / (1 + t): nothing overflows, and nothing cancels (the second
-// term is at most half the first). A gate of +inf, where a * t would be NaN, gives +inf:
-// a positive gate enters a as 128 at most, where t is 0 already; -inf gives NaN, as
-// g / (1 + exp(-g)) does, and so does NaN, through max(g, 0). t = 2^y * (1 + c), y the rounded product of -a
-// and log2 e and c the error of that rounding, from one more multiply-add, times ln 2.
+// silu(g) for eight fp16 values. With n = -|g| and t = e^n <= 1, silu(g) =
+// max(g, 0) + n * t / (1 + t): nothing overflows, and nothing cancels (the second
+// term is at most half the first). t = 2^y * (1 + c), y the rounded product of n and
+// log2 e; c = n - y * ln 2, with ln 2 in two parts, takes back y's rounding and that of
+// the constant, which the size of n multiplies (with ln 2 in one part the result was off by 15
+// half steps at g = -60). c is below 2^-17, so that what 1 + c leaves out is nothing.
 // With ex2.approx within 2^-22 and rcp.approx within 2^-23 the result is within 10
-// half steps of fp32 (a Newton step on the reciprocal would take one away and cost
-// 5% of the time).
+// half steps of fp32: 4 and 2, and one each for 1 + c, n * t, 1 + t and the last step (a
+// Newton step on the reciprocal would take one away and cost 5% of the time). Below
+// g = -87.3 t leaves fp32's normal range and counts as 0.
+// A gate of +inf, where n * t would be NaN, gives +inf: a positive gate enters n as -128 at
+// least, where t is 0 already; -inf gives NaN, as g / (1 + exp(-g)) does, and so does
+// NaN, through max(g, 0).
 __device__ __forceinline__ Oct silu8(const uint4& u) {
-  constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
+  constexpr float kLog2e = 1.44269504088896340736f;
+  constexpr float kLn2 = 0.69314718055994530942f;
+  constexpr float kLn2Low = static_cast<float>(0.69314718055994530942 - static_cast<double>(kLn2));
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
   Oct o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 g = *reinterpret_cast<const __half2*>(&w[i]);
-    const float2 af = __half22float2(__hmax2(__hneg2(g), __hmin2(g, __float2half2_rn(128.0f))));
-    const float2 gf = __half22float2(__hmax2_nan(g, __float2half2_rn(0.0f)));
-    const uint64_t a = pair2(af.x, af.y);
-    const uint64_t y = mul2(a, pair2(-kLog2e, -kLog2e));
-    const uint64_t c = mul2(fma2(a, pair2(kLog2e, kLog2e), y), pair2(-kLn2, -kLn2));
+    const float2 nf = __half22float2(__hmin2(h[i], __hmax2(__hneg2(h[i]), __float2half2_rn(-128.0f))));
+    const float2 gf = __half22float2(__hmax2_nan(h[i], __float2half2_rn(0.0f)));
+    const uint64_t n = pair2(nf.x, nf.y);
+    const uint64_t y = mul2(n, pair2(kLog2e, kLog2e));
+    const uint64_t c = fma2(y, pair2(-kLn2Low, -kLn2Low), fma2(y, pair2(-kLn2, -kLn2), n));
     const float2 y1 = split2(y);
     float e0, e1, r0, r1;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(y1.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(y1.y));
     uint64_t t = pair2(e0, e1);
     t = fma2(t, c, t);
-    const uint64_t d = add2(t, pair2(1.0f, 1.0f));
-    const float2 d1 = split2(d);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d1.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1.y));
-    const uint64_t r = pair2(r0, r1);                 // -1 / (1 + t)
-    o.v[i] = fma2(mul2(a, t), r, pair2(gf.x, gf.y));
+    const float2 d1 = split2(add2(t, pair2(1.0f, 1.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d1.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1.y));
+    o.v[i] = fma2(mul2(n, t), pair2(r0, r1), pair2(gf.x, gf.y));
   }
   return o;
 }
