@@ -401,8 +401,9 @@ int int8_scaled_matmul(const int8_t* Xq, const float* x_scale, const int8_t* Wq,
 //   n_adapters  in : 1 to 4096
 //   Y0          in : fp16 [M][N]
 //   Y           out: fp16 [M][N]; Y0 itself (in place), or apart from it
-//   workspace      : int8_adapter_add_workspace_size(...) bytes, 256-byte aligned;
-//                    contents on entry are ignored. Calls that may overlap on the GPU
+//   workspace      : int8_adapter_add_workspace_size(...) bytes, 256-byte aligned. The
+//                    size does not decrease in any argument: one of the largest call's
+//                    size serves the smaller calls too. Contents on entry are ignored. Calls that may overlap on the GPU
 //                    need workspaces of their own. int8_device_status(workspace) tells
 //                    whether a bounded device-side wait of the call gave up.
 size_t int8_adapter_add_workspace_size(int M, int N, int K, int n_adapters, int R);

@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include "int8mm.h"
@@ -1401,27 +1402,30 @@ cudaError_t launch_large(AdapterArgs p, cudaStream_t s) {
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Fills in the workspace's parts (offsets from ws) and returns its size.
-size_t carve(AdapterArgs* p, uint8_t* ws) {
+// Each fills in the parts of the workspace that its form uses (offsets from ws) and
+// returns their size.
+size_t carve_small(AdapterArgs* p, uint8_t* ws) {
+  // About 512 columns per CTA (four warps of four 32-column steps each), half as many
+  // for the larger ranks, whose steps do not all fit into the registers; at most kMaxSlices.
+  const int cols = p->R <= 32 ? 512 : 256;
+  const int s = (p->K + cols - 1) / cols;
+  p->S = s < kMaxSlices ? s : kMaxSlices;
+  p->slice = ((p->K + p->S - 1) / p->S + 127) / 128 * 128;
   p->head = reinterpret_cast<int32_t*>(ws);
+  p->part = reinterpret_cast<float*>(ws + 256);
+  return 256 + up256(static_cast<size_t>(p->S) * p->M * p->R * 4);
+}
+
+size_t carve_large(AdapterArgs* p, uint8_t* ws) {
   size_t off = 256;
-  if (p->M <= small_tokens(p->R, p->n)) {
-    // About 512 columns per CTA (four warps of four 32-column steps each), half as many
-    // for the larger ranks, whose steps do not all fit into the registers; at most kMaxSlices.
-    const int cols = p->R <= 32 ? 512 : 256;
-    const int s = (p->K + cols - 1) / cols;
-    p->S = s < kMaxSlices ? s : kMaxSlices;
-    p->slice = ((p->K + p->S - 1) / p->S + 127) / 128 * 128;
-    p->part = reinterpret_cast<float*>(ws + off);
-    return off + up256(static_cast<size_t>(p->S) * p->M * p->R * 4);
-  }
   auto take = [&](size_t bytes) {
     uint8_t* at = ws + off;
     off += up256(bytes);
     return at;
   };
   const size_t M = p->M;
-  p->tiles = reinterpret_cast<int4*>(take(static_cast<size_t>(max_groups(*p, 128)) * sizeof(int4)));
+  p->head = reinterpret_cast<int32_t*>(ws);
+  p->tiles = reinterpret_cast<int4*>(take(static_cast<size_t>(max_groups(*p, kTile)) * sizeof(int4)));
   p->perm = reinterpret_cast<int32_t*>(take(M * 4));
   p->factor = reinterpret_cast<float*>(take(M * 4));
   p->hi = reinterpret_cast<__half*>(take(M * p->R * 2));
@@ -1447,12 +1451,23 @@ extern "C" {
 
 size_t int8_adapter_add_workspace_size(int M, int N, int K, int n_adapters, int R) {
   if (check_adapter(M, N, K, n_adapters, R) != I8MM_OK) return 0;
+  // The most that a call with no larger arguments needs, in either form: the form for few
+  // tokens needs more than the other (1 MB at most), and up to fewer tokens the larger the
+  // rank, so a call's own need would shrink as its batch or rank grows.
   AdapterArgs p{};
   p.M = M;
   p.K = K;
   p.n = n_adapters;
   p.R = R;
-  return carve(&p, nullptr);
+  size_t most = carve_large(&p, nullptr);
+  for (const int top : {16, 32, 64, kMaxRank}) {   // the ranks that small_tokens tells apart
+    p.R = R < top ? R : top;
+    const int tokens = small_tokens(p.R, n_adapters);
+    p.M = M < tokens ? M : tokens;
+    const size_t need = carve_small(&p, nullptr);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 int int8_adapter_add(const void* X, const void* A, const void* B, const int32_t* adapter_idx,
@@ -1487,10 +1502,14 @@ int int8_adapter_add(const void* X, const void* A, const void* B, const int32_t*
   p.K = K;
   p.n = n_adapters;
   p.R = R;
-  carve(&p, static_cast<uint8_t*>(workspace));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return abi_cuda_fail("adapter kernel launch",
-                       M <= small_tokens(R, n_adapters) ? launch_small(p, s) : launch_large(p, s));
+  const bool small = M <= small_tokens(R, n_adapters);
+  if (small)
+    carve_small(&p, ws);
+  else
+    carve_large(&p, ws);
+  return abi_cuda_fail("adapter kernel launch", small ? launch_small(p, s) : launch_large(p, s));
 }
 
 }  // extern "C"
