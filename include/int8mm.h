@@ -380,12 +380,19 @@ int int8_swiglu_quantize_rows(const void* GU, const float* s_rcp, int M, int I, 
 //                    int8_swiglu_quantize_rows, int8_quantize_act_rows, ...)
 //   Wq, w_scale in : int8 [N][K], fp32 [N] (int8_quantize_weight_rows, ...)
 //   Y           out: fp16 [M][N]
-//   status      out: device int32, 4-byte aligned, or NULL. I8MM_ERR_TIMEOUT is stored
-//                    there if a bounded device-side wait gave up; otherwise it is left
-//                    alone, so the caller clears it once and reads it when it likes.
+//   status      out: device int32, 4-byte aligned. I8MM_ERR_TIMEOUT is stored there if a
+//                    bounded device-side wait gave up; otherwise it is left alone, so the
+//                    caller clears it once and reads it when it likes. NULL: a word of the
+//                    library's on that device, which int8_scaled_matmul_status reads.
 int int8_scaled_matmul(const int8_t* Xq, const float* x_scale, const int8_t* Wq,
                        const float* w_scale, int M, int N, int K, void* Y, int32_t* status,
                        i8mm_stream_t stream);
+
+// Whether a wait gave up in any int8_scaled_matmul without a status of its own on the
+// current device (or int8_debug_gemm_i32, which has none), in work that is complete, since
+// the last such question: I8MM_OK or I8MM_ERR_TIMEOUT, which is cleared with the answer.
+// Synchronises `stream`; other streams' products are waited for by the caller.
+int int8_scaled_matmul_status(i8mm_stream_t stream);
 
 // Low-rank adapters of many requests, added to a projection's result: with
 // a = adapter_idx[i],  Y[i] = fp16(Y0[i] + scaling[a] * B[a] . (A[a] . X[i])),
@@ -463,6 +470,9 @@ int int8_debug_gemm_i32(const int8_t* Xq, const int8_t* Wq, int M, int N, int K,
  * synchronises `stream` and reads *status. Nothing faults or hangs.
  */
 int int8_selftest_wait_timeout(int32_t* status, i8mm_stream_t stream);
+/* The same with the word of int8_scaled_matmul_status as *status: that of the CTA pair
+ * GEMM where `gemm` is not 0, else that of the kernel for fewer tokens. */
+int int8_selftest_product_status(int gemm, i8mm_stream_t stream);
 
 /*
  * Reads the device status word a previous int8_mixed_matmul left in its

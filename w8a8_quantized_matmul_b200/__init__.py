@@ -52,6 +52,7 @@ __all__ = [
     "int8_rmsnorm_quantize_rows",
     "int8_swiglu_quantize_rows",
     "int8_scaled_matmul",
+    "int8_scaled_matmul_status",
     "int8_adapter_add_workspace_size",
     "int8_adapter_add",
     "Int8mmError",
@@ -663,8 +664,8 @@ def int8_swiglu_quantize_rows(GU, s_rcp=None, Z=None, Zq=True, z_scale=None, str
 def int8_scaled_matmul(Xq, x_scale, Wq, w_scale, Y=None, status=None, stream=None):
     """Y fp16 [M, N] = (Xq . Wq^T) * x_scale * w_scale / 127^2 of INT8 rows [M, K], [N, K].
 
-    status (int32 [1], or None) receives I8MM_ERR_TIMEOUT if a device-side wait
-    gave up and is left alone otherwise. Returns Y."""
+    status (int32 [1]) receives I8MM_ERR_TIMEOUT if a device-side wait gave up and is
+    left alone otherwise; None: int8_scaled_matmul_status tells. Returns Y."""
     M, K = Xq.shape
     N = Wq.shape[0]
     dev = _device(Xq, "Xq")
@@ -683,6 +684,16 @@ def int8_scaled_matmul(Xq, x_scale, Wq, w_scale, Y=None, status=None, stream=Non
           load().int8_scaled_matmul(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
                                     M, N, K, Y.data_ptr(), _at(status), _raw_stream(dev)))
     return Y
+
+
+def int8_scaled_matmul_status(stream=None) -> int:
+    """I8MM_ERR_TIMEOUT if a wait gave up in an int8_scaled_matmul without a status of its
+    own on the current device (the stream's, if given) since the last such question, else 0.
+    Synchronises the stream; other streams' products are waited for by the caller."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_scaled_matmul_status()
+    return int(load().int8_scaled_matmul_status(_stream(None)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -733,3 +744,9 @@ def selftest_wait_timeout(stream=None) -> int:
           load().int8_selftest_wait_timeout(_ptr(status), _stream(stream)))
     torch.cuda.synchronize()
     return int(status.item())
+
+
+def selftest_product_status(gemm, stream=None) -> None:
+    """The same wait, recorded where a product without a status of its own records one (the
+    CTA pair GEMM, or the kernel for fewer tokens): int8_scaled_matmul_status tells."""
+    check("int8_selftest_product_status", load().int8_selftest_product_status(bool(gemm), _stream(stream)))

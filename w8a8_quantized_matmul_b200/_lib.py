@@ -62,10 +62,12 @@ PROTOTYPES = {
                                         _vp]),
     "int8_swiglu_quantize_rows": (_i, [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp]),
     "int8_scaled_matmul": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "int8_scaled_matmul_status": (_i, [_vp]),
     "int8_adapter_add_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "int8_adapter_add": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz,
                               _vp]),
     "int8_selftest_wait_timeout": (_i, [_vp, _vp]),
+    "int8_selftest_product_status": (_i, [_i, _vp]),
     "int8_device_status": (_i, [_vp, _vp]),
     "int8_noalloc_device_status": (_i, [_vp]),
     "int8_status_string": (ctypes.c_char_p, [_i]),

@@ -90,8 +90,11 @@ struct Cfg {
   static constexpr int SMEM_BYTES = 1024 /*alignment slack*/ + BAR_OFF + BAR_BYTES;
 };
 
+// Where a product without a status word of its own records a wait that gave up.
+static __device__ int32_t g_gemm_status;
+
 __device__ __forceinline__ void record_error(int32_t* status, int code) {
-  if (status) atomicCAS(status, 0, code);
+  atomicCAS(status ? status : &g_gemm_status, 0, code);
 }
 
 __device__ __forceinline__ void epi_sync() {
@@ -639,6 +642,10 @@ bool make_tmap_3d_sw128(CUtensorMap* m, const void* base, CUtensorMapDataType dt
 }
 
 int device_sm_count(int dev) { return sm_count(dev); }
+
+cudaError_t gemm_status_word(int32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_gemm_status);
+}
 
 // CTA pairs whenever there is more than one 128-row block of output rows.
 cudaError_t launch_gemm_mixed(const GemmArgs& a, cudaStream_t s) {

@@ -110,6 +110,12 @@ bool make_tmap_3d_sw128(CUtensorMap* m, const void* base, CUtensorMapDataType dt
                         uint64_t cols, uint64_t rows, uint64_t mats, uint32_t box_rows);
 int device_sm_count(int dev);
 
+// The words of the current device in which a product records a wait that gave up
+// where its caller gave it no status word: of the CTA pair GEMM (gemm_sm100.cu) and of
+// the kernel for fewer tokens (scaled_matmul.cu).
+cudaError_t gemm_status_word(int32_t** word);
+cudaError_t weight_stream_status_word(int32_t** word);
+
 // Least dynamic shared memory of a CTA of a cluster kernel that allocates `cols` TMEM
 // columns. A CTA waits in the allocation until the columns are free, and a cluster's
 // CTAs wait for one another while they hold theirs; were more columns asked for

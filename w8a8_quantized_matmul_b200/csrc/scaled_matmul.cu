@@ -41,11 +41,14 @@ constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 10;
 constexpr int kThreads = 192;
 
+// Where a product without a status word of its own records a wait that gave up.
+static __device__ int32_t g_stream_status;
+
 struct StreamArgs {
   const float* x_scale;   // [M]
   const float* w_scale;   // [N]
   __half* Y;              // [M][N]
-  int32_t* status;        // or nullptr
+  int32_t* status;        // or nullptr: g_stream_status
   int M, N, K;
   int tok;                // tokens of a block, the MMA's N: a multiple of 16, at most kMaxTok
   int split;              // S
@@ -100,6 +103,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int32_t* stop = reinterpret_cast<volatile int32_t*>(tslot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* const status = a.status ? a.status : &g_stream_status;
   const int S = a.split;
   const int rank = static_cast<int>(cluster_ctarank());
   const int n0 = static_cast<int>(blockIdx.x / S) * kRows;
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     if (lane == 0) {
       for (int j = 0; j < nb; ++j) {
         const int s = j % a.stages;
-        if (!wait_or_give_up(&empty[s], ((j / a.stages) & 1) ^ 1, stop, a.status)) break;
+        if (!wait_or_give_up(&empty[s], ((j / a.stages) & 1) ^ 1, stop, status)) break;
         uint8_t* w = sm + s * L.stage;
         const int k = (rank + j * S) * kKB;
         mbar_arrive_expect_tx(&full[s], L.stage);
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     const uint32_t idesc = make_idesc(2 /*s32*/, 1 /*signed*/, kRows, a.tok);
     for (int j = 0; j < nb && ok; ++j) {
       const int s = j % a.stages;
-      ok = __all_sync(0xffffffffu, wait_or_give_up(&full[s], (j / a.stages) & 1, stop, a.status));
+      ok = __all_sync(0xffffffffu, wait_or_give_up(&full[s], (j / a.stages) & 1, stop, status));
       if (!ok) break;
       const uint64_t w = sw128_kmajor_desc(smem_addr(sm + s * L.stage));
       const uint64_t x = sw128_kmajor_desc(smem_addr(sm + s * L.stage + kWBytes));
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
     named_bar_sync(1, 128);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     if (S == 1) {
-      ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, a.status));
+      ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, status));
       tc_fence_after();
       const int np = n0 + (nl & ~1);
       const float wo = __shfl_xor_sync(0xffffffffu, ws, 1);
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) weight_stream_kernel(const __grid_co
       if (warp >= 2) {
         const int q = warp & 3;
         if (c0 == 0) {
-          ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, a.status));
+          ok = __all_sync(0xffffffffu, wait_or_give_up(done, 0, stop, status));
           tc_fence_after();
           if (!ok) let_copies_land();               // they go where the partials will
           named_bar_sync(1, 128);
@@ -375,6 +379,10 @@ cudaError_t launch_scaled(const GemmArgs& g, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t weight_stream_status_word(int32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_stream_status);
+}
+
 }  // namespace i8mm
 
 using namespace i8mm;
@@ -403,4 +411,26 @@ extern "C" int int8_scaled_matmul(const int8_t* Xq, const float* x_scale, const 
   g.status = status;
   g.ld = 64;
   return abi_cuda_fail("product kernel launch", launch_scaled(g, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int int8_scaled_matmul_status(i8mm_stream_t stream) {
+  int st = abi_check_device();
+  if (st != I8MM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t* word[2] = {};
+  int32_t h[2] = {};
+  cudaError_t e = gemm_status_word(&word[0]);
+  if (e == cudaSuccess) e = weight_stream_status_word(&word[1]);
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    e = cudaMemcpyAsync(&h[i], word[i], 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  // Only a word that holds something is cleared: nothing is lost that comes in meanwhile.
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    if (h[i] != 0) e = cudaMemsetAsync(word[i], 0, 4, s);
+  if (e == cudaSuccess && (h[0] != 0 || h[1] != 0)) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();   // do not leave it for the next launch
+    return abi_cuda_fail("status read", e);
+  }
+  return h[0] != 0 ? h[0] : h[1];
 }

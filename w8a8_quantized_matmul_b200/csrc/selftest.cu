@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "int8mm.h"
+#include "kernels.cuh"
 #include "ptx.cuh"
 
 namespace i8mm {
@@ -37,4 +38,13 @@ extern "C" int int8_selftest_wait_timeout(int32_t* status, i8mm_stream_t stream)
   if (cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return I8MM_ERR_CUDA;
   i8mm::wait_timeout_kernel<<<1, 32, 0, s>>>(status);
   return cudaGetLastError() == cudaSuccess ? I8MM_OK : I8MM_ERR_CUDA;
+}
+
+extern "C" int int8_selftest_product_status(int gemm, i8mm_stream_t stream) {
+  const int st = i8mm::abi_check_device();
+  if (st != I8MM_OK) return st;
+  int32_t* word = nullptr;
+  const cudaError_t e = gemm ? i8mm::gemm_status_word(&word) : i8mm::weight_stream_status_word(&word);
+  if (e != cudaSuccess) return i8mm::abi_cuda_fail("address of the status word", e);
+  return int8_selftest_wait_timeout(word, stream);
 }
