@@ -626,6 +626,10 @@ int max_groups(const AdapterArgs& p, int per) {
 }
 
 cudaError_t launch_small(AdapterArgs p, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int sms = device_sm_count(dev);
   const int groups = max_groups(p, kChunk);
   const size_t seen = (static_cast<size_t>(p.n) + 1) * 4;
   const int blocks = (p.N + kNBlock - 1) / kNBlock;
@@ -649,7 +653,7 @@ cudaError_t launch_small(AdapterArgs p, cudaStream_t s) {
     // As many CTAs as run at a time (one per possible group at least), each with its
     // share of a group's column blocks: a CTA finds its group and t once.
     const int fit = static_cast<int>(228 * 1024 / (bytes + (vec ? 3 : 20) * 1024));   // by shared memory
-    const int at_once = 148 * (fit < 1 ? 1 : fit > 5 ? 5 : fit);
+    const int at_once = sms * (fit < 1 ? 1 : fit > 5 ? 5 : fit);
     const int64_t most = static_cast<int64_t>(groups) * blocks;
     const int ctas = at_once < groups ? groups : static_cast<int>(at_once < most ? at_once : most);
     return launch_pdl(vec ? reinterpret_cast<const void*>(small_expand_kernel<RB, true>)
@@ -657,10 +661,10 @@ cudaError_t launch_small(AdapterArgs p, cudaStream_t s) {
                       dim3(ctas), kSmallThreads, bytes, s, args);
   };
   using std::integral_constant;
-  cudaError_t e = p.R <= 16   ? shrink(integral_constant<int, 1>{})
-                  : p.R <= 32 ? shrink(integral_constant<int, 2>{})
-                  : p.R <= 64 ? shrink(integral_constant<int, 4>{})
-                              : shrink(integral_constant<int, 8>{});
+  e = p.R <= 16   ? shrink(integral_constant<int, 1>{})
+      : p.R <= 32 ? shrink(integral_constant<int, 2>{})
+      : p.R <= 64 ? shrink(integral_constant<int, 4>{})
+                  : shrink(integral_constant<int, 8>{});
   if (e != cudaSuccess) return e;
   return p.R <= 16   ? expand(integral_constant<int, 0>{})
          : p.R <= 32 ? expand(integral_constant<int, 1>{})
