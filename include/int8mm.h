@@ -410,9 +410,10 @@ int int8_scaled_matmul_status(i8mm_stream_t stream);
 //   Y           out: fp16 [M][N]; Y0 itself (in place), or apart from it
 //   workspace      : int8_adapter_add_workspace_size(...) bytes, 256-byte aligned. The
 //                    size does not decrease in any argument: one of the largest call's
-//                    size serves the smaller calls too. Contents on entry are ignored. Calls that may overlap on the GPU
-//                    need workspaces of their own. int8_device_status(workspace) tells
-//                    whether a bounded device-side wait of the call gave up.
+//                    size serves the smaller calls too. Contents on entry are ignored.
+//                    Calls that may overlap on the GPU need workspaces of their own.
+//                    int8_device_status(workspace) tells whether a bounded device-side
+//                    wait of the call gave up.
 size_t int8_adapter_add_workspace_size(int M, int N, int K, int n_adapters, int R);
 int int8_adapter_add(const void* X, const void* A, const void* B, const int32_t* adapter_idx,
                      const float* scaling, int M, int N, int K, int n_adapters, int R,
